@@ -204,14 +204,6 @@ def _own(s):
             return carve.scan_step(s["x"], s["g"], s["h0"], **opt), s["h0"]
         h, h_T, ws = carve.scan_fwd(s["x"], s["g"], s["h0"], cu_seqlens=cu,
                                     training=train, **opt)
-        rest = c["T"] % 64 if c["ragged"] and c["T"] > 64 * c["B"] else 0
-        if rest:
-            # The call leaves zeros in the rows behind the last sequence; the
-            # plain form lets its state decay on through them, so that is what
-            # has to be compared: those rows once more, without inputs.
-            carve.scan_fwd(torch.zeros_like(s["x"][None, -rest:]),
-                           s["g"][None, -rest:], h_T[-1:],
-                           h=h[None, -rest:], want_state=False, **opt)
         if not train:
             return h, h_T
         gr = carve.scan_bwd(s["x"], s["g"], s["d_h"], ws, dh_T=s["dh_T"],
@@ -318,6 +310,7 @@ def _plain_scan(s):
     xi[first] += a[first] * s["h0"][some]
     ac = a.clone()
     ac[first] = 0
+    ac[end:] = 0  # rows of no sequence: no state runs on through them
     xi[end:] = 0
     h = _scan_in_place(ac, xi, s["longest"])
     h_T = s["h0"].clone()
