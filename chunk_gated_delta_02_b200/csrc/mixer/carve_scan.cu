@@ -729,6 +729,8 @@ struct BwdTile {
   };
 };
 
+// The status word stays what the forward that filled the workspace has made
+// it, unless this pass goes wrong too: its gradients come from kept states.
 template <typename IO, bool SEG, bool ACT, bool COMP>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a) {
   after_the_last();
@@ -778,17 +780,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a) {
     const bool small = a.B < kKeepCu;
     const bool ok = small ? offsets_kept(a.cu, a.B, a.T, sm.cu) : offsets_ok(a.cu, a.B, a.T);
     if (small) p.b.cu = sm.cu;
-    if (blockIdx.x == 0 && threadIdx.x == 0)
-      *a.status = ok ? CARVE_OK : CARVE_ERR_INVALID_ARG;
     if (!ok) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = CARVE_ERR_INVALID_ARG;
       cp_async_wait<0>();
       return;
     }
     ask_states(a, p, a.keep_h0);
     ask_states(a, p, a.dh_T);
     copy_empty(a, p, a.dh_T, a.dh0);
-  } else if (a.status && blockIdx.x == 0 && threadIdx.x == 0) {
-    *a.status = CARVE_OK;
   }
 
   start_exchange(sm.ex, p.ncl);

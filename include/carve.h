@@ -307,7 +307,9 @@ carve_status carve_decode_step(const carve_shape* shape,
  *     that decrease or leave [0, T] are found on the device: the call then
  *     writes CARVE_ERR_INVALID_ARG to the status word and no output.
  *     Every call that takes a workspace writes the status word (CARVE_OK
- *     otherwise), so the workspace needs no clearing before it.
+ *     otherwise), so the workspace needs no clearing before it.  Only
+ *     carve_scan_bwd, whose workspace a forward has filled, writes nothing
+ *     but errors: after forward and backward the word tells of both.
  *   - Outputs (states that are updated in place among them) overlap neither
  *     inputs nor one another.
  *   - Rows of no sequence (before cu_seqlens[0], from cu_seqlens[B] on)
@@ -519,7 +521,8 @@ carve_status carve_conv_step(const carve_conv_shape* shape, const void* x,
  * bounded device-side wait gave up; the kernel then skipped the rest of its
  * work and left its outputs unspecified; CARVE_ERR_WORKSPACE when a
  * backward was given a workspace the other kernel family wrote).  The word
- * is sticky until carve_reset_status.
+ * is sticky until carve_reset_status, or until an operator around the core
+ * that writes CARVE_OK (see there) is given the workspace.
  *
  * Every wait of the tensor-core kernels on a copy, an MMA or the partner
  * CTA gives up after about 1 s (2^31 cycles).  Two environment variables

@@ -1,0 +1,46 @@
+"""GPU: the status word that the operators around the core leave in a
+workspace (no GPU fault is involved: bounded waits run out through the
+test-only knobs of the library, on good memory)."""
+import pytest
+import torch
+
+from chunk_gated_delta_02_b200 import carve
+
+from _mixer import offsets
+
+pytestmark = pytest.mark.gpu
+
+
+def status(ws):
+    return carve.STATUS[carve.get_status(ws)]
+
+
+def rn(*shape, dtype=torch.float32, seed=1):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=gen).to(dtype).cuda()
+
+
+def stall(monkeypatch, on):
+    """Block 1 keeps its pair of tile 1 to itself: its cluster's waits run out
+    after 2e5 cycles."""
+    for name, value in (("CARVE_TEST_WAIT_CYCLES", "200000"), ("CARVE_TEST_STALL_BLOCK", "1")):
+        monkeypatch.setenv(name, value) if on else monkeypatch.delenv(name)
+
+
+@pytest.mark.parametrize("packed", [False, True], ids=["dense", "packed"])
+def test_backward_keeps_the_forwards_error(monkeypatch, packed):
+    x, g = rn(1, 4096, 64), -0.1 * rn(1, 4096, 64, seed=2).abs()
+    cu = None
+    if packed:
+        x, g, cu = x[0], g[0], offsets([4096])
+    stall(monkeypatch, True)
+    _, _, ws = carve.scan_fwd(x, g, cu_seqlens=cu, training=True)
+    torch.cuda.synchronize()
+    stall(monkeypatch, False)
+    gr = carve.scan_bwd(x, g, x, ws, cu_seqlens=cu)
+    assert status(ws) == "CARVE_ERR_TIMEOUT"
+    assert gr["dg"].isnan().any()  # of the states that the forward kept
+    # a forward starts anew
+    carve.scan_fwd(x, g, cu_seqlens=cu, training=True, workspace=ws)
+    carve.scan_bwd(x, g, x, ws, cu_seqlens=cu)
+    assert status(ws) == "CARVE_OK"
