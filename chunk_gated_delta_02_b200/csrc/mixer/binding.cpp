@@ -169,6 +169,7 @@ Tensor workspace(const MaybeTensor& mine, size_t bytes, const char* entry, const
   if (mine->scalar_type() != at::kByte || mine->device() != k.dev || !mine->is_contiguous() ||
       mine->numel() < (int64_t)bytes)
     bad("workspace must be ", (int64_t)bytes, " contiguous bytes (uint8) on ", k.dev.str());
+  if ((uintptr_t)mine->data_ptr() % 16) ok(CARVE_ERR_WORKSPACE, entry);
   return *mine;
 }
 
@@ -245,7 +246,7 @@ py::tuple scan_fwd(const Tensor& x, const Tensor& g, const MaybeTensor& h0,
   const carve_scan_shape s = scan_shape(b, k, scale, comp, !mine, pitch_of(x, "x", b.lead),
                                         pitch(g, "g", k, x.sizes(), b.lead));
   need(h0, "h0", kState, b.state, k.dev);
-  if (training || cu)
+  if (training || cu || ws)
     ws = workspace(ws, carve_scan_workspace_bytes(&s, cu.has_value(), training),
                    "carve_scan_workspace_bytes", k);
   const Tensor h = like(k, x, mine, "h");
@@ -640,8 +641,9 @@ h0 [B, ...] fp32 or None; h like x; h_T [B, ...] fp32 (None with
 want_state=False).  decay_scale > 0: g holds raw decay logits a, the log-decay
 is -decay_scale * softplus(a).  complement: the input enters as
 (1 - exp(g_t)) x_t.  With training=True the returned workspace holds what
-scan_bwd needs; it is None where nothing needs one.  The status word of a
-packed call (get_status(workspace)) tells whether cu_seqlens was valid.)");
+scan_bwd needs; it is None where nothing needs one and none is given (256 bytes,
+uint8, without training).  Its status word (get_status(workspace)) tells whether
+cu_seqlens was valid and whether a wait gave up.)");
   def<scan_bwd>(m, "scan_bwd",
             {arg("x"), arg("g"), arg("d_h"), arg("workspace"), arg("dh_T", none),
              arg("cu_seqlens", none), arg("want_dh0", yes), arg("out", none),

@@ -1184,7 +1184,7 @@ carve_status carve_scan_fwd(const carve_scan_shape* shape,
   }
   ScanArgs a = scan_args(s, p);
   a.x = x; a.g = g; a.h0 = h0; a.h = h; a.h_T = h_T; a.cu = cu_seqlens;
-  a.status = training || cu_seqlens ? static_cast<uint32_t*>(workspace) : nullptr;
+  a.status = status_word(workspace, workspace_bytes);
   if (training) {
     a.keep = (float*)((char*)workspace + w.keep);
     a.keep_h0 = p.seg ? (float*)((char*)workspace + w.keep_h0) : nullptr;

@@ -17,6 +17,12 @@ inline bool opt_ptr_ok(const void* p) { return p == nullptr || aligned16(p); }
 inline bool flag_ok(int v) { return v == 0 || v == 1; }
 inline bool dtype_ok(int d) { return d == CARVE_BF16 || d == CARVE_FP32; }
 
+// The status word of a workspace, NULL where there is no room for one (calls
+// that need a workspace have refused that before).
+inline uint32_t* status_word(void* ws, size_t bytes) {
+  return ptr_ok(ws) && bytes >= kHeaderBytes ? static_cast<uint32_t*>(ws) : nullptr;
+}
+
 // Token indices (and a tile past the last) stay inside 32 bits; element
 // offsets are formed in 64.
 constexpr int64_t kMaxTokens = (1LL << 31) - (1 << 16);

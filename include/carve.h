@@ -307,7 +307,9 @@ carve_status carve_decode_step(const carve_shape* shape,
  *     that decrease or leave [0, T] are found on the device: the call then
  *     writes CARVE_ERR_INVALID_ARG to the status word and no output.
  *     Every call that takes a workspace writes the status word (CARVE_OK
- *     otherwise), so the workspace needs no clearing before it.  Only
+ *     otherwise), so the workspace needs no clearing before it; calls that
+ *     need none write it into one that they are given all the same (aligned,
+ *     256 bytes or more; a smaller one is not touched).  Only
  *     carve_scan_bwd, whose workspace a forward has filled, writes nothing
  *     but errors: after forward and backward the word tells of both.
  *   - Outputs (states that are updated in place among them) overlap neither

@@ -44,3 +44,27 @@ def test_backward_keeps_the_forwards_error(monkeypatch, packed):
     carve.scan_fwd(x, g, cu_seqlens=cu, training=True, workspace=ws)
     carve.scan_bwd(x, g, x, ws, cu_seqlens=cu)
     assert status(ws) == "CARVE_OK"
+
+
+def used(n=256):
+    """A workspace that something else has been in."""
+    return torch.full((n,), 0x55, dtype=torch.uint8, device="cuda")
+
+
+def test_inference_scan_reports_to_a_workspace_it_is_given(monkeypatch):
+    x, g, ws = rn(1, 4096, 64), -0.1 * rn(1, 4096, 64, seed=2).abs(), used()
+    stall(monkeypatch, True)
+    h, _, got = carve.scan_fwd(x, g, workspace=ws)
+    torch.cuda.synchronize()
+    stall(monkeypatch, False)
+    assert got is ws and h.isnan().any() and status(ws) == "CARVE_ERR_TIMEOUT"
+    h, _, _ = carve.scan_fwd(x, g, workspace=ws)
+    assert h.isfinite().all() and status(ws) == "CARVE_OK"
+    empty, ws = x[:, :0], used()
+    carve.scan_fwd(empty, empty, workspace=ws)
+    assert status(ws) == "CARVE_OK"
+    for bad in (used(255), ws.cpu()):
+        with pytest.raises(ValueError, match="workspace"):
+            carve.scan_fwd(x, g, workspace=bad)
+    with pytest.raises(carve.CarveError, match="WORKSPACE"):  # not on 16 bytes
+        carve.scan_fwd(x, g, workspace=used(264)[8:])
