@@ -423,8 +423,8 @@ py::tuple conv_fwd(const Tensor& x, const Tensor& w, const MaybeTensor& bias,
                    const MaybeTensor& state, const MaybeTensor& cu, bool silu,
                    const MaybeTensor& mine, bool want_state, MaybeTensor ws) {
   const Conv c(x, w, bias, state, cu, silu, !mine);
-  if (cu)
-    ws = workspace(ws, carve_conv_workspace_bytes(&c.s, 1, 0), "carve_conv_workspace_bytes", c.k);
+  if (cu || ws)
+    ws = workspace(ws, carve_conv_workspace_bytes(&c.s, cu.has_value(), 0), "carve_conv_workspace_bytes", c.k);
   const Tensor y = like(c.k, x, mine, "y");
   apart(mine, "y", {&x, &w, the(bias), the(state), the(cu), the(ws)});
   MaybeTensor state_T;
@@ -690,9 +690,8 @@ x [B, T, ...] (bf16 or fp32; a multiple of 8 channels in the trailing
 dimensions), or packed [T, ...] with cu_seqlens [N + 1] int32; w [C, W] with
 W = 2, 3 or 4 taps; bias [C] or None; state [B, W - 1, ...] the inputs before
 each sequence (None: zeros), state_T the same after it (None with
-want_state=False).  silu=True: act(z) = z sigmoid(z).  A packed call that is
-given a workspace (256 bytes, uint8) leaves its status word there for
-get_status.)");
+want_state=False).  silu=True: act(z) = z sigmoid(z).  A call that is given a
+workspace (256 bytes, uint8) leaves its status word there for get_status.)");
   def<conv_bwd>(m, "conv_bwd",
             {arg("x"), arg("w"), arg("dy"), arg("bias", none), arg("state", none),
              arg("dstate_T", none), arg("cu_seqlens", none), arg("silu", no),

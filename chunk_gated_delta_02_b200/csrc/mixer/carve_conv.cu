@@ -196,6 +196,10 @@ __device__ __forceinline__ bool packed_ok(const ConvArgs& a) {
   return ok;
 }
 
+__device__ __forceinline__ void dense_ok(const ConvArgs& a) {
+  if (a.status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = CARVE_OK;
+}
+
 // Rows [t, end) of a warp that belong to no sequence.
 template <typename IO, int V>
 __device__ __forceinline__ void fill_rows(const ConvArgs& a, void* out, int t,
@@ -227,6 +231,8 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm<V>) conv_fwd_kernel(ConvAr
   if (a.cu) {
     if (!packed_ok(a)) return;
     copy_empty<IO, V>(a, W - 1, c, on, a.state, a.state_T);
+  } else {
+    dense_ok(a);
   }
   const Bounds b{a.cu, a.T, a.B};
   const int64_t first = ((int64_t)blockIdx.y * kWarps + warp) * a.run;
@@ -317,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<V>) conv_bwd_kernel(ConvAr
   if (a.cu) {
     if (!packed_ok(a)) return;
     copy_empty<IO, V>(a, W - 1, c, on, a.dstate_T, a.dstate);
-  } else if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-    *a.status = CARVE_OK;
+  } else {
+    dense_ok(a);
   }
   const Bounds b{a.cu, a.T, a.B};
   const int64_t first = ((int64_t)blockIdx.y * kWarps + warp) * a.run;
@@ -438,12 +444,14 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<V>) conv_bwd_kernel(ConvAr
 
 // dw, dbias: the blocks' partials, 32 of them a block of threads, summed by
 // the warps over every eighth and then over the warps (an order fixed by the
-// shape).  A bad packed call has none.
+// shape).  A bad packed call has none.  A call without tokens has no blocks in
+// front of this one and gets its status word here.
 __global__ void __launch_bounds__(kThreads) conv_dw_kernel(ConvArgs a, int W, int blocks,
                                                            float* dw, float* db) {
   after_the_last();
   __shared__ float sum[kWarps][32];
   if (a.cu && *a.status != CARVE_OK) return;
+  if (blocks == 0) dense_ok(a);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cols = a.C * (W + 1), i = blockIdx.x * 32 + lane;
   float t = 0.f;
@@ -559,13 +567,13 @@ size_t conv_ws(const carve_conv_shape& s, const ConvPlan& p, bool backward) {
 
 ConvArgs conv_args(const carve_conv_shape& s, const ConvPlan& p,
                    const int32_t* cu, const void* x, const void* w,
-                   const void* bias, void* ws) {
+                   const void* bias, void* ws, size_t ws_bytes) {
   ConvArgs a{};
   a.B = s.B; a.T = s.T; a.C = s.C; a.silu = s.silu; a.fill = s.fill_rest;
   a.rows = p.rows; a.run = p.run;
   a.xp = s.x_pitch ? s.x_pitch : s.C;
   a.cu = cu; a.x = x; a.w = w; a.bias = bias;
-  a.status = static_cast<uint32_t*>(ws);
+  a.status = status_word(ws, ws_bytes);
   return a;
 }
 
@@ -640,10 +648,12 @@ carve_status carve_conv_fwd(const carve_conv_shape* shape,
     return CARVE_ERR_WORKSPACE;
   cudaStream_t cs = (cudaStream_t)stream;
   cudaError_t e;
+  ConvArgs a = conv_args(s, p, cu_seqlens, x, w, bias, workspace, workspace_bytes);
   if (!cu_seqlens && s.T == 0) {
+    static_assert(CARVE_OK == 0, "the status word by memset");
     e = pass_state(s, state, state_T, cs);
+    if (e == cudaSuccess && a.status) e = cudaMemsetAsync(a.status, 0, sizeof(*a.status), cs);
   } else {
-    ConvArgs a = conv_args(s, p, cu_seqlens, x, w, bias, workspace);
     a.state = state; a.y = y; a.state_T = state_T;
     e = launch_conv(kFwd, s, p.pairs, a, dim3(p.cols, p.blocks), cs);
   }
@@ -672,7 +682,7 @@ carve_status carve_conv_bwd(const carve_conv_shape* shape,
       workspace_bytes < conv_ws(s, p, true))
     return CARVE_ERR_WORKSPACE;
   cudaStream_t cs = (cudaStream_t)stream;
-  ConvArgs a = conv_args(s, p, cu_seqlens, x, w, bias, workspace);
+  ConvArgs a = conv_args(s, p, cu_seqlens, x, w, bias, workspace, workspace_bytes);
   a.state = state; a.dy = dy; a.dstate_T = dstate_T; a.dx = dx; a.dstate = dstate;
   a.part = (float*)((char*)workspace + kHeaderBytes);
   const bool none = !cu_seqlens && s.T == 0;
@@ -693,7 +703,7 @@ carve_status carve_conv_step(const carve_conv_shape* shape, const void* x,
   if (!ptr_ok(x) || !ptr_ok(w) || !ptr_ok(state) || !ptr_ok(y) || !opt_ptr_ok(bias))
     return CARVE_ERR_INVALID_ARG;
   ConvPlan p{};
-  ConvArgs a = conv_args(s, p, nullptr, x, w, bias, nullptr);
+  ConvArgs a = conv_args(s, p, nullptr, x, w, bias, nullptr, 0);
   a.state_T = state; a.y = y;
   const int64_t blocks = ((int64_t)s.B * s.C / 4 + 127) / 128;
   if (blocks >= (1LL << 31)) return CARVE_ERR_UNSUPPORTED;

@@ -68,3 +68,39 @@ def test_inference_scan_reports_to_a_workspace_it_is_given(monkeypatch):
             carve.scan_fwd(x, g, workspace=bad)
     with pytest.raises(carve.CarveError, match="WORKSPACE"):  # not on 16 bytes
         carve.scan_fwd(x, g, workspace=used(264)[8:])
+
+
+@pytest.mark.parametrize("T", [0, 30])
+@pytest.mark.parametrize("packed", [False, True], ids=["dense", "packed"])
+def test_convolution_writes_the_word(packed, T):
+    x, w, cu = rn(2, T, 16), rn(16, 4), None
+    if packed:
+        x, cu = x.reshape(2 * T, 16), offsets([T, T])
+    size = carve.lib().carve_conv_workspace_bytes
+    shape = carve.ConvShape(2, x.shape[-2], 16, 4, carve.CARVE_FP32, 0, 0, 0, 0)
+    ws, wb = used(size(shape, int(packed), 0)), used(size(shape, int(packed), 1))
+    y, _ = carve.conv_fwd(x, w, cu_seqlens=cu, workspace=ws)
+    assert status(ws) == "CARVE_OK" and y.shape == x.shape
+    gr = carve.conv_bwd(x, w, x, cu_seqlens=cu, workspace=wb)
+    assert status(wb) == "CARVE_OK"
+    assert T or (gr["dw"] == 0).all()
+
+
+def test_convolution_without_tokens_captured():
+    """A copy and a memset in front of a kernel."""
+    x, w, s = rn(2, 0, 16), rn(16, 4), rn(2, 3, 16)
+    ws, wb = used(), used(4096)
+    call = lambda: (carve.conv_fwd(x, w, None, s, workspace=ws)[1],  # noqa: E731
+                    carve.conv_bwd(x, w, x, None, s, 2 * s, workspace=wb))
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        state, gr = call()
+    for t in (state, gr["dstate"], gr["dw"]):
+        t.fill_(7)
+    for t in (ws, wb):
+        t.fill_(0x55)
+    graph.replay()
+    assert torch.equal(state, s) and torch.equal(gr["dstate"], 2 * s) and (gr["dw"] == 0).all()
+    assert status(ws) == status(wb) == "CARVE_OK"
