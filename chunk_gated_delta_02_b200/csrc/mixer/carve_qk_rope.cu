@@ -308,8 +308,10 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) rope_bwd_kernel(RopeArgs 
 // dw[i] = sum over the partials of the blocks of q (blockIdx.y 0) or k, 32
 // columns a block: 8 lanes read a row of them, every 128th row each, and the
 // sums of the 128 are added in their order.
-__global__ void __launch_bounds__(1024) rope_dw_kernel(RopeArgs a, float* dwq, float* dwk) {
+__global__ void __launch_bounds__(1024) rope_dw_kernel(RopeArgs a, float* dwq, float* dwk,
+                                                       uint32_t* status) {
   after_the_last();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = CARVE_OK;
   __shared__ float sum[128][33];
   const bool isk = blockIdx.y;
   const int row = threadIdx.x / 8, c = threadIdx.x % 8 * 4;
@@ -433,7 +435,7 @@ extern "C" {
 size_t carve_qk_rope_workspace_bytes(const carve_rope_shape* shape) {
   if (check_rope(shape) != CARVE_OK) return 0;
   const RopeArgs a = rope_args(*shape, true);
-  return align256((size_t)(a.q.blocks + a.k.blocks + 1) * shape->D * 4);
+  return kHeaderBytes + align256((size_t)(a.q.blocks + a.k.blocks + 1) * shape->D * 4);
 }
 
 carve_status carve_qk_rope_fwd(const carve_rope_shape* shape, const void* q,
@@ -479,13 +481,14 @@ carve_status carve_qk_rope_bwd(const carve_rope_shape* shape, const void* q,
   RopeArgs a = rope_args(s, true);
   a.q.x = q; a.k.x = k; a.pos = pos; a.freqs = freqs; a.q.w = w_q; a.k.w = w_k;
   a.q.dy = dq_out; a.k.dy = dk_out; a.q.out = dq; a.k.out = dk;
-  a.part = sums ? static_cast<float*>(workspace) : nullptr;
+  a.part = sums ? (float*)((char*)workspace + kHeaderBytes) : nullptr;
   cudaStream_t cs = (cudaStream_t)stream;
   if (s.N > 0 && launch_rope(true, a, s.dtype, cs) != cudaSuccess)
     return CARVE_ERR_CUDA;
   if (sums) {
     if (launch_all<rope_dw_kernel>(dim3((s.D + 31) / 32, 2), 1024, 0, cs, 1, a,
-                                   w_q ? dw_q : nullptr, w_k ? dw_k : nullptr) != cudaSuccess)
+                                   w_q ? dw_q : nullptr, w_k ? dw_k : nullptr,
+                                   static_cast<uint32_t*>(workspace)) != cudaSuccess)
       return CARVE_ERR_CUDA;
   }
   return CARVE_OK;

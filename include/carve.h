@@ -308,8 +308,9 @@ carve_status carve_decode_step(const carve_shape* shape,
  *     writes CARVE_ERR_INVALID_ARG to the status word and no output.
  *     Every call that takes a workspace writes the status word (CARVE_OK
  *     otherwise), so the workspace needs no clearing before it; calls that
- *     need none write it into one that they are given all the same (aligned,
- *     256 bytes or more; a smaller one is not touched).  Only
+ *     need none (carve_scan_fwd, carve_conv_fwd) write it into one that they
+ *     are given all the same (aligned, 256 bytes or more; a smaller one is
+ *     not touched).  Only
  *     carve_scan_bwd, whose workspace a forward has filled, writes nothing
  *     but errors: after forward and backward the word tells of both.
  *   - Outputs (states that are updated in place among them) overlap neither
@@ -426,8 +427,8 @@ typedef struct {
   int64_t q_pitch, k_pitch; /* elements between tokens; 0 = H * D */
 } carve_rope_shape;
 
-/* Workspace bytes of carve_qk_rope_bwd (partial weight gradients); 0 for an
- * invalid shape. */
+/* Workspace bytes of carve_qk_rope_bwd (the header with the status word and
+ * partial weight gradients); 0 for an invalid shape. */
 size_t carve_qk_rope_workspace_bytes(const carve_rope_shape* shape);
 
 /*
@@ -448,7 +449,7 @@ carve_status carve_qk_rope_fwd(const carve_rope_shape* shape, const void* q,
  * Reverse mode: dq_out, dk_out [N, H, D] dtype contiguous are the gradients
  * of the outputs; dq, dk [N, H, D] dtype contiguous; dw_q, dw_k [D] fp32,
  * written when the weight is given (and may be NULL when it is not).  The
- * workspace may be NULL when neither weight is given.
+ * workspace may be NULL when neither weight is given, and is then not touched.
  */
 carve_status carve_qk_rope_bwd(const carve_rope_shape* shape, const void* q,
                                const void* k, const int32_t* pos,

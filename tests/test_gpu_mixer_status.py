@@ -104,3 +104,21 @@ def test_convolution_without_tokens_captured():
     graph.replay()
     assert torch.equal(state, s) and torch.equal(gr["dstate"], 2 * s) and (gr["dw"] == 0).all()
     assert status(ws) == status(wb) == "CARVE_OK"
+
+
+@pytest.mark.parametrize("N", [0, 50])
+def test_rotations_backward_writes_the_word(N):
+    """Through the C entry point: the binding keeps this workspace to itself."""
+    lib, f32 = carve.lib(), carve.CARVE_FP32
+    q, w, d = rn(N, 2, 32), rn(32, seed=2), rn(N, 2, 32, seed=3)
+    want = carve.qk_rope_bwd(q, None, None, None, d, None, w)
+    shape = carve.RopeShape(N, 2, 0, 32, 0, f32, 1e-6, 0, 0, 0, 0)
+    ws = used(lib.carve_qk_rope_workspace_bytes(shape) + 256)
+    dq, dw = torch.empty_like(q), torch.empty(32, device="cuda")
+    p = lambda t: t.data_ptr() or None  # noqa: E731
+    rc = lib.carve_qk_rope_bwd(shape, p(q), None, None, None, p(w), None, p(d), None, p(ws),
+                               ws.numel() - 256, p(dq), None, p(dw), None,
+                               torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and status(ws) == "CARVE_OK"
+    assert torch.equal(dq, want["dq"]) and torch.equal(dw, want["dw_q"])
+    assert (ws[-256:] == 0x55).all()
