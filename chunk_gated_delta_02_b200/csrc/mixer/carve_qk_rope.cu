@@ -108,7 +108,7 @@ __device__ __forceinline__ void turn(Q& u, Q& v, const Q& c, const Q& s, bool in
 
 __device__ __forceinline__ float inverse_norm(float ss, const RopeArgs& a) {
   const float m = fmaf(ss, a.inv_n, a.eps);
-  return m > 0.f ? rsqrtf(m) : 0.f;
+  return m == 0.f ? 0.f : rsqrtf(m);  // NaN stays: the whole row becomes NaN
 }
 __device__ __forceinline__ Q scaled(const Q& q, float f) {
   return Q{{mul2(q.p[0], both(f)), mul2(q.p[1], both(f))}};

@@ -410,8 +410,10 @@ carve_status carve_scan_step(const carve_scan_shape* shape, const void* x,
  * for the RD / 2 pairs (i, j = i + RD / 2), or (2 i, 2 i + 1) with
  * interleaved != 0, of the first RD elements; the others keep n.  The angle
  * is formed and reduced in fp64, so far positions keep full accuracy.  A
- * row whose norm is 0 with eps = 0 gives zeros (and a zero gradient).  The
- * sum of squares is formed in fp32 and has to be finite.
+ * row whose norm is 0 with eps = 0 gives zeros (and a zero gradient).  A NaN
+ * makes its whole row NaN.  The sum of squares is formed in fp32: it has to be
+ * finite (elements below 1e18).  With eps = 0 the squares of elements below
+ * 1e-19 lose bits, and a row of elements below 1e-23 counts as one of norm 0.
  *
  * N tokens (batch and time flattened), HQ query and HK key heads (HK may be
  * 0), D a multiple of 16 up to 256, RD a multiple of 16 up to D (0: no
