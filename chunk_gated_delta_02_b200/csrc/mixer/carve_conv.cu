@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<V>) conv_bwd_kernel(ConvAr
 
 // dw, dbias: the blocks' partials, 32 of them a block of threads, summed by
 // the warps over every eighth and then over the warps (an order fixed by the
-// shape).  A bad packed call has none.  A call without tokens has no blocks in
+// shape and the number of SMs).  A bad packed call has none.  A call without tokens has no blocks in
 // front of this one and gets its status word here.
 __global__ void __launch_bounds__(kThreads) conv_dw_kernel(ConvArgs a, int W, int blocks,
                                                            float* dw, float* db) {

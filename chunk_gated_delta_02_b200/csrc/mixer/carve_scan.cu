@@ -1067,12 +1067,15 @@ ScanWs scan_ws(const carve_scan_shape& s, const ScanPlan& p, bool training) {
 }
 
 // Clusters of n blocks that the device holds at once, two blocks an SM: fewer
-// than the SMs would take, as a cluster stays within a group of SMs.  Asked
-// for once (the devices of a machine are alike, and no result depends on it).
+// than the SMs would take, as a cluster stays within a group of SMs.  Each
+// device is asked once.  The answer decides the size of the clusters, and that
+// the rounding: alone, a block carries the state it has walked from tile to
+// tile; in a cluster it is A h + H of whole tiles.
 template <auto kernel>
 int clusters_held(int n, size_t smem) {
-  static std::atomic<int> held[kMaxCluster + 1];
-  int v = held[n].load();
+  static std::atomic<int> held[kDevices][kMaxCluster + 1];
+  const int dev = kept_device();
+  int v = dev >= 0 ? held[dev][n].load() : 0;
   if (v > 0) return v;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
@@ -1080,9 +1083,9 @@ int clusters_held(int n, size_t smem) {
   if (allow_smem<kernel>(smem) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess || v < 1) {
     cudaGetLastError();
-    v = 2 * sm_count() / n;
+    return 2 * sm_count() / n;  // this call's guess, not kept
   }
-  held[n].store(v);
+  if (dev >= 0) held[dev][n].store(v);
   return v;
 }
 

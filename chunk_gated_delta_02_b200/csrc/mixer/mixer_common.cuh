@@ -34,16 +34,26 @@ inline bool pitch_ok(int64_t p, int64_t width) {
   return p == 0 || (p >= width && p % 8 == 0);
 }
 
+// What is asked of a device once is kept by its number, up to this many.
+constexpr int kDevices = 64;
+// The number of the current device, -1 if it has none that answers are kept by.
+inline int kept_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev < kDevices ? dev : -1;
+}
+
+// The current device's SMs.  They decide how calls are cut up, and so in which
+// order partial results are added.
 inline int sm_count() {
-  static int n = 0;  // every device of a B200 machine has the same count
-  if (n == 0) {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess &&
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) ==
-            cudaSuccess)
-      n = v;
-  }
-  return n > 0 ? n : 148;
+  static std::atomic<int> kept[kDevices];
+  const int at = kept_device();
+  int n = at >= 0 ? kept[at].load() : 0, dev = 0;
+  if (n > 0) return n;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    return 148;
+  if (at >= 0) kept[at].store(n);
+  return n;
 }
 
 // Lets the kernel use its shared memory: asked for once a device.
@@ -51,15 +61,13 @@ template <auto kernel>
 cudaError_t allow_smem(size_t smem) {
   if (smem <= 48 * 1024) return cudaSuccess;
   static std::atomic<uint64_t> asked{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev > 63 || !(asked.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) asked.fetch_or(1ull << dev);
-  }
-  return cudaSuccess;
+  static_assert(kDevices <= 64, "a bit each");
+  const int at = kept_device();
+  if (at >= 0 && asked.load() >> at & 1) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && at >= 0) asked.fetch_or(1ull << at);
+  return e;
 }
 
 inline void cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, dim3 grid,

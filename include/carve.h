@@ -318,7 +318,10 @@ carve_status carve_decode_step(const carve_shape* shape,
  *   - Rows of no sequence (before cu_seqlens[0], from cu_seqlens[B] on)
  *     are left as they were, or set to zero with fill_rest != 0.
  *   - Results do not depend on timing: no floating-point atomics, and sums
- *     over tokens are formed in an order fixed by the shape.
+ *     over tokens are formed in an order fixed by the shape and the device
+ *     (its SMs, and the clusters of blocks that it holds at once).  Devices
+ *     that differ in these, or parts of one that is shared out, may round
+ *     differently.
  * B * T (T for a packed batch) must be below 2^31 - 2^16, pitches and
  * channels of a token at most 2^22 elements.
  *
