@@ -7,12 +7,19 @@ Each .cu file under csrc/ (and its folders) is compiled to an object in csrc/_bu
 when it or any header is newer), then linked into
 chunk_gated_delta_02_b200/libcarve.so next to the bindings.
 csrc/mixer/binding.cpp, host code only, becomes _mixer.so there (g++ against
-the headers of the installed torch, linked to that libcarve.so).
+the headers of the installed torch, linked to that libcarve.so); it is rebuilt
+for another torch or Python as well.  libcarve.so needs nvcc alone: where torch,
+the C++ compiler or the Python headers are missing, it is built and the binding
+is left out with a note on stderr.
 """
 import glob
+import importlib.metadata
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +28,7 @@ OBJ = os.path.join(CSRC, "_build")
 LIB = os.path.join(HERE, "libcarve.so")
 BINDING_SRC = os.path.join(CSRC, "mixer", "binding.cpp")
 BINDING = os.path.join(HERE, "_mixer.so")
+BINDING_MADE = os.path.join(OBJ, "_mixer.txt")  # what that was built for
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -42,9 +50,38 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _binding_command(out):
-    import sysconfig
+def _binding_lacks():
+    """What the binding cannot be built without and this machine has not, or
+    None."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if shutil.which(CXX) is None:
+        return "the C++ compiler %s" % CXX
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "the Python headers"
+    return None
 
+
+def _binding_for():
+    """What a binding is built for, beside its sources."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # not installed as a package
+        torch = "unknown"
+    return "torch %s, python %s\n" % (torch, sysconfig.get_config_var("SOABI"))
+
+
+def _binding_stale():
+    if _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "carve.h")]):
+        return True
+    try:
+        with open(BINDING_MADE) as f:
+            return f.read() != _binding_for()
+    except OSError:
+        return True
+
+
+def _binding_command(out):
     import torch
     from torch.utils import cpp_extension
     include = cpp_extension.include_paths() + [
@@ -85,10 +122,17 @@ def build(force=False, verbose=False):
         tmp = LIB + ".tmp.%d" % os.getpid()
         run([NVCC] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs)
         os.replace(tmp, LIB)
-    if force or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "carve.h")]):
+    if force or _binding_stale():
+        lacks = _binding_lacks()
+        if lacks:
+            print("note: %s is not here, so %s is not built; %s is complete"
+                  % (lacks, os.path.basename(BINDING), LIB), file=sys.stderr)
+            return LIB
         tmp = BINDING + ".tmp.%d" % os.getpid()
         run(_binding_command(tmp))
         os.replace(tmp, BINDING)
+        with open(BINDING_MADE, "w") as f:
+            f.write(_binding_for())
     return LIB
 
 
