@@ -173,6 +173,13 @@ Tensor workspace(const MaybeTensor& mine, size_t bytes, const char* entry, const
   return *mine;
 }
 
+// Tells autograd that a call has written into a caller's tensors: a backward
+// pass that has kept one then refuses to run instead of reading new values.
+void written(Others ts) {
+  for (const Tensor* t : ts)
+    if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // What a call returns: tensors or None, in a tuple or under names.
 PyObject* wrapped(const Tensor* t) {
   if (t) return THPVariable_Wrap(*t);
@@ -256,6 +263,7 @@ py::tuple scan_fwd(const Tensor& x, const Tensor& g, const MaybeTensor& h0,
   ok(carve_scan_fwd(&s, iin(cu), x.data_ptr(), g.data_ptr(), fin(h0), h.data_ptr(), fout(h_T),
                     out(ws), ws ? ws->numel() : 0, training, k.stream()),
      "carve_scan_fwd");
+  written({the(mine), the(ws)});
   return tuple_of({&h, the(h_T), the(ws)});
 }
 
@@ -290,6 +298,7 @@ py::dict scan_bwd(const Tensor& x, const Tensor& g, const Tensor& d_h, const May
                     ws->data_ptr(), ws->numel(), dx.data_ptr(), dg.data_ptr(), fout(dh0),
                     k.stream()),
      "carve_scan_bwd");
+  if (mine) written({&dx, &dg, the(dh0)});
   return dict_of({{"dx", &dx}, {"dg", &dg}, {"dh0", the(dh0)}});
 }
 
@@ -308,6 +317,7 @@ Tensor scan_step(const Tensor& x, const Tensor& g, const Tensor& h, const MaybeT
   ok(carve_scan_step(&s, x.data_ptr(), g.data_ptr(), h.data_ptr<float>(), o.data_ptr(),
                      k.stream()),
      "carve_scan_step");
+  written({&h, the(mine)});
   return o;
 }
 
@@ -356,6 +366,7 @@ py::tuple qk_rope_fwd(const Tensor& q, const MaybeTensor& key, const MaybeTensor
                        static_cast<const double*>(in(freqs)), in(w_q), in(w_k), q_out.data_ptr(),
                        out(k_out), r.k.stream()),
      "carve_qk_rope_fwd");
+  written({the(q_mine), the(k_mine)});
   return tuple_of({&q_out, the(k_out)});
 }
 
@@ -395,6 +406,7 @@ py::dict qk_rope_bwd(const Tensor& q, const MaybeTensor& key, const MaybeTensor&
                        ws ? ws->numel() : 0, dq.data_ptr(), out(dk), fout(dw_q), fout(dw_k),
                        k.stream()),
      "carve_qk_rope_bwd");
+  if (mine) written({&dq, the(dk), the(dw_q), the(dw_k)});
   return dict_of({{"dq", &dq}, {"dk", the(dk)}, {"dw_q", the(dw_q)}, {"dw_k", the(dw_k)}});
 }
 
@@ -432,6 +444,7 @@ py::tuple conv_fwd(const Tensor& x, const Tensor& w, const MaybeTensor& bias,
   ok(carve_conv_fwd(&c.s, iin(cu), x.data_ptr(), w.data_ptr(), in(bias), in(state), y.data_ptr(),
                     out(state_T), out(ws), ws ? ws->numel() : 0, c.k.stream()),
      "carve_conv_fwd");
+  written({the(mine), the(ws)});
   return tuple_of({&y, the(state_T)});
 }
 
@@ -464,6 +477,8 @@ py::dict conv_bwd(const Tensor& x, const Tensor& w, const Tensor& dy, const Mayb
                     dy.data_ptr(), in(dstate_T), ws->data_ptr(), ws->numel(), dx.data_ptr(),
                     fout(dw), fout(dbias), out(dstate), k.stream()),
      "carve_conv_bwd");
+  if (mine) written({&dx, the(dw), the(dbias), the(dstate)});
+  written({the(ws)});
   return dict_of({{"dx", &dx}, {"dw", the(dw)}, {"dbias", the(dbias)}, {"dstate", the(dstate)}});
 }
 
@@ -484,6 +499,7 @@ Tensor conv_step(const Tensor& x, const Tensor& w, const Tensor& state, const Ma
   ok(carve_conv_step(&s, x.data_ptr(), w.data_ptr(), in(bias), state.data_ptr(), y.data_ptr(),
                      k.stream()),
      "carve_conv_step");
+  written({&state, the(mine)});
   return y;
 }
 
