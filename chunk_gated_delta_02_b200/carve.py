@@ -404,4 +404,4 @@ def carve(q, k, v, g, bx, w, u_down, u_up, L, S0=None, m0=None,
 # The operators around the chunk core (their wrappers use the names above).
 from .mixer import (  # noqa: E402
     conv, conv_bwd, conv_fwd, conv_step, qk_rope, qk_rope_bwd, qk_rope_fwd,
-    rope_freqs, scan, scan_bwd, scan_fwd, scan_step)
+    rope_freqs, scan, scan_bwd, scan_fwd, scan_step, scan_workspace)

@@ -14,9 +14,19 @@ the call reads.  Here are the autograd wrappers.
 
 To capture a training step into a CUDA graph, capture the ``_fwd`` and ``_bwd``
 calls: capturing ``backward()`` while an eager graph of the same leaves lives
-can end the process inside torch.  The wrappers do not read the status word of
-a packed call; scan_fwd's workspace, or one given to conv_fwd, has it.
+can end the process inside torch.
+
+A packed call with bad offsets writes no output: what it returns is memory as it
+was allocated.  No call reads the status word back, which would wait for the
+GPU; the wrappers hand on a workspace, whose word ``carve.get_status`` reads:
+
+    ws = carve.scan_workspace(x, cu_seqlens)
+    h, h_T = carve.scan(x, g, cu_seqlens=cu_seqlens, workspace=ws)
+    y, state_T = carve.conv(x, w, cu_seqlens=cu_seqlens, workspace=ws2)  # 256 bytes
+    carve.get_status(ws)
 """
+import ctypes
+
 import torch
 from torch.autograd.function import once_differentiable
 
@@ -54,11 +64,12 @@ class ScanFunction(torch.autograd.Function):
     """Autograd wrapper of scan_fwd / scan_bwd (see scan)."""
 
     @staticmethod
-    def forward(ctx, x, g, h0, cu_seqlens, decay_scale, complement):
+    def forward(ctx, x, g, h0, cu_seqlens, decay_scale, complement, workspace):
         ctx.set_materialize_grads(False)
         train = any(ctx.needs_input_grad)
         h, h_T, ws = scan_fwd(x, g, h0, cu_seqlens, training=train,
-                              decay_scale=decay_scale, complement=complement)
+                              workspace=workspace, decay_scale=decay_scale,
+                              complement=complement)
         if train:
             ctx.save_for_backward(x, g, cu_seqlens, ws)
             ctx.opt = dict(decay_scale=decay_scale, complement=complement)
@@ -73,12 +84,33 @@ class ScanFunction(torch.autograd.Function):
         gr = scan_bwd(x, g, d_h, ws, None if dh_T is None else
                       dh_T.contiguous(), cu_seqlens,
                       want_dh0=ctx.needs_input_grad[2], **ctx.opt)
-        return gr["dx"], gr["dg"], gr["dh0"], None, None, None
+        return gr["dx"], gr["dg"], gr["dh0"], None, None, None, None
 
 
-def scan(x, g, h0=None, cu_seqlens=None, decay_scale=0.0, complement=False):
-    """Differentiable gated linear scan; returns (h, h_T) (see scan_fwd)."""
-    return ScanFunction.apply(x, g, h0, cu_seqlens, decay_scale, complement)
+def scan(x, g, h0=None, cu_seqlens=None, decay_scale=0.0, complement=False,
+         workspace=None):
+    """Differentiable gated linear scan; returns (h, h_T) (see scan_fwd).  The
+    backward pass reads a workspace (scan_workspace) that is given: keep it for
+    this call until then."""
+    return ScanFunction.apply(x, g, h0, cu_seqlens, decay_scale, complement,
+                              workspace)
+
+
+def scan_workspace(x, cu_seqlens=None, training=True):
+    """A workspace (uint8) for a scan over x: scan_fwd and scan take it, and its
+    status word can be read afterwards."""
+    from . import carve
+    lead = 2 if cu_seqlens is None else 1
+    shape = carve.ScanShape(
+        B=x.shape[0] if lead == 2 else cu_seqlens.numel() - 1,
+        T=x.shape[lead - 1], C=x.shape[lead:].numel(),
+        dtype=carve.CARVE_BF16 if x.dtype == torch.bfloat16 else carve.CARVE_FP32)
+    with torch.cuda.device(x.device):
+        n = carve.lib().carve_scan_workspace_bytes(
+            ctypes.byref(shape), int(lead == 1), int(bool(training)))
+        if n == 0:
+            raise carve.CarveError("carve_scan_workspace_bytes", 2)
+        return torch.empty(n, dtype=torch.uint8, device=x.device)
 
 
 def rope_freqs(dims, theta=10000.0, device="cuda"):
@@ -121,11 +153,12 @@ class ConvFunction(torch.autograd.Function):
     """Autograd wrapper of conv_fwd / conv_bwd (see conv)."""
 
     @staticmethod
-    def forward(ctx, x, w, bias, state, cu_seqlens, silu):
+    def forward(ctx, x, w, bias, state, cu_seqlens, silu, workspace):
         ctx.set_materialize_grads(False)
         ctx.silu = silu
         ctx.save_for_backward(x, w, bias, state, cu_seqlens)
-        return conv_fwd(x, w, bias, state, cu_seqlens, silu)
+        return conv_fwd(x, w, bias, state, cu_seqlens, silu,
+                        workspace=workspace)
 
     @staticmethod
     @once_differentiable
@@ -137,10 +170,11 @@ class ConvFunction(torch.autograd.Function):
                       dstate_T.contiguous(), cu_seqlens, ctx.silu)
         return (gr["dx"], gr["dw"].to(w.dtype),
                 None if bias is None else gr["dbias"].to(bias.dtype),
-                None if state is None else gr["dstate"], None, None)
+                None if state is None else gr["dstate"], None, None, None)
 
 
-def conv(x, w, bias=None, state=None, cu_seqlens=None, silu=False):
+def conv(x, w, bias=None, state=None, cu_seqlens=None, silu=False,
+         workspace=None):
     """Differentiable short causal convolution; returns (y, state_T) (see
-    conv_fwd)."""
-    return ConvFunction.apply(x, w, bias, state, cu_seqlens, silu)
+    conv_fwd, which the workspace goes to)."""
+    return ConvFunction.apply(x, w, bias, state, cu_seqlens, silu, workspace)
