@@ -246,16 +246,18 @@ carve_scan_shape scan_shape(const Batch& b, const Common& k, double scale, bool 
 }
 
 py::tuple scan_fwd(const Tensor& x, const Tensor& g, const MaybeTensor& h0,
-                   const MaybeTensor& cu, bool training, MaybeTensor ws,
+                   const MaybeTensor& cu, bool training, const MaybeTensor& mine_ws,
                    const MaybeTensor& mine, bool want_state, double scale, bool comp) {
   const Common k(x, "x");
   const Batch b(x, "x", cu, k, 0);
   const carve_scan_shape s = scan_shape(b, k, scale, comp, !mine, pitch_of(x, "x", b.lead),
                                         pitch(g, "g", k, x.sizes(), b.lead));
   need(h0, "h0", kState, b.state, k.dev);
-  if (training || cu || ws)
-    ws = workspace(ws, carve_scan_workspace_bytes(&s, cu.has_value(), training),
+  MaybeTensor ws;
+  if (training || cu || mine_ws)
+    ws = workspace(mine_ws, carve_scan_workspace_bytes(&s, cu.has_value(), training),
                    "carve_scan_workspace_bytes", k);
+  apart(mine_ws, "workspace", {&x, &g, the(h0), the(cu)});
   const Tensor h = like(k, x, mine, "h");
   apart(mine, "h", {&x, &g, the(h0), the(cu), the(ws)});
   MaybeTensor h_T;
@@ -284,6 +286,7 @@ py::dict scan_bwd(const Tensor& x, const Tensor& g, const Tensor& d_h, const May
   need(dh_T, "dh_T", kState, b.state, k.dev);
   if (!ws) bad("scan_bwd needs the workspace of a training forward");
   workspace(ws, carve_scan_workspace_bytes(&s, cu.has_value(), 1), "carve_scan_workspace_bytes", k);
+  apart(ws, "workspace", {&x, &g, &d_h, the(dh_T), the(cu)});
   const Tensor dx = like(k, x, mine ? given(item(mine, "dx"), "dx") : MaybeTensor(), "dx");
   const Tensor dg = like(k, x, mine ? given(item(mine, "dg"), "dg") : MaybeTensor(), "dg");
   MaybeTensor dh0 = item(mine, "dh0");
@@ -433,10 +436,12 @@ struct Conv {
 
 py::tuple conv_fwd(const Tensor& x, const Tensor& w, const MaybeTensor& bias,
                    const MaybeTensor& state, const MaybeTensor& cu, bool silu,
-                   const MaybeTensor& mine, bool want_state, MaybeTensor ws) {
+                   const MaybeTensor& mine, bool want_state, const MaybeTensor& mine_ws) {
   const Conv c(x, w, bias, state, cu, silu, !mine);
-  if (cu || ws)
-    ws = workspace(ws, carve_conv_workspace_bytes(&c.s, cu.has_value(), 0), "carve_conv_workspace_bytes", c.k);
+  MaybeTensor ws;
+  if (cu || mine_ws)
+    ws = workspace(mine_ws, carve_conv_workspace_bytes(&c.s, cu.has_value(), 0), "carve_conv_workspace_bytes", c.k);
+  apart(mine_ws, "workspace", {&x, &w, the(bias), the(state), the(cu)});
   const Tensor y = like(c.k, x, mine, "y");
   apart(mine, "y", {&x, &w, the(bias), the(state), the(cu), the(ws)});
   MaybeTensor state_T;
@@ -450,13 +455,14 @@ py::tuple conv_fwd(const Tensor& x, const Tensor& w, const MaybeTensor& bias,
 
 py::dict conv_bwd(const Tensor& x, const Tensor& w, const Tensor& dy, const MaybeTensor& bias,
                   const MaybeTensor& state, const MaybeTensor& dstate_T, const MaybeTensor& cu,
-                  bool silu, const std::optional<py::dict>& mine, MaybeTensor ws) {
+                  bool silu, const std::optional<py::dict>& mine, const MaybeTensor& mine_ws) {
   const Conv c(x, w, bias, state, cu, silu, !mine);
   const Common& k = c.k;
   need(dy, "dy", k.type, x.sizes(), k.dev);
   need(dstate_T, "dstate_T", k.type, c.b.state, k.dev);
-  ws = workspace(ws, carve_conv_workspace_bytes(&c.s, cu.has_value(), 1),
-                 "carve_conv_workspace_bytes", k);
+  const MaybeTensor ws = workspace(
+      mine_ws, carve_conv_workspace_bytes(&c.s, cu.has_value(), 1), "carve_conv_workspace_bytes", k);
+  apart(mine_ws, "workspace", {&x, &w, &dy, the(bias), the(state), the(dstate_T), the(cu)});
   const Tensor dx = like(k, x, mine ? given(item(mine, "dx"), "dx") : MaybeTensor(), "dx");
   MaybeTensor dw = item(mine, "dw"), dbias = item(mine, "dbias"), dstate = item(mine, "dstate");
   if (mine) {

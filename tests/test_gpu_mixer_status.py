@@ -122,3 +122,24 @@ def test_rotations_backward_writes_the_word(N):
     assert rc == 0 and status(ws) == "CARVE_OK"
     assert torch.equal(dq, want["dq"]) and torch.equal(dw, want["dw_q"])
     assert (ws[-256:] == 0x55).all()
+
+
+def test_workspace_over_an_input_is_refused():
+    """One allocation, seen as bytes and as what a call reads."""
+    raw = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    x = raw[4096:4096 + 2 * 70 * 16 * 4].view(torch.float32).view(2, 70, 16)
+    clear, w = rn(2, 70, 16), rn(16, 4)
+    over, beside = raw[:8192], raw[40000:]
+    state = raw[:2 * 3 * 16 * 4].view(torch.float32).view(2, 3, 16)
+    calls = [lambda ws: carve.scan_fwd(x, clear, workspace=ws),
+             lambda ws: carve.scan_fwd(clear, x, training=True, workspace=ws),
+             lambda ws: carve.conv_fwd(x, w, workspace=ws),
+             lambda ws: carve.conv_fwd(clear, w, state=state, workspace=ws),
+             lambda ws: carve.conv_bwd(clear, w, x, workspace=ws),
+             lambda ws: carve.conv_bwd(clear, w, clear, state=state, workspace=ws),
+             lambda ws: carve.scan_bwd(clear, -clear.abs(), x, ws)]
+    carve.scan_fwd(clear, -clear.abs(), training=True, workspace=beside)
+    for call in calls:
+        with pytest.raises(ValueError, match="workspace overlaps"):
+            call(over)
+        call(beside)
