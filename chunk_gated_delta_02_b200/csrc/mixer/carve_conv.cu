@@ -84,11 +84,11 @@ __device__ __forceinline__ Vec<V> addc(const Vec<V>& a, const Vec<V>& b) {
   for (int h = 0; h < V; ++h) r.p[h] = add2(a.p[h], b.p[h]);
   return r;
 }
-template <int V>
+template <typename IO, int V>
 __device__ __forceinline__ Vec<V> sigmoids(const Vec<V>& z) {
   Vec<V> r;
 #pragma unroll
-  for (int h = 0; h < V; ++h) r.p[h] = make_float2(fast_sigmoid(z.p[h].x), fast_sigmoid(z.p[h].y));
+  for (int h = 0; h < V; ++h) r.p[h] = sigmoid_of<IO>(z.p[h]);
   return r;
 }
 
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm<V>) conv_fwd_kernel(ConvAr
       auto token = [&](int i) {
         const Vec<V> x = ldc<IO, V>(rows, i * kCh<V>);
         Vec<V> z = taps.z(win, x);
-        if (a.silu) z = mulc(z, sigmoids(z));
+        if (a.silu) z = mulc(z, sigmoids<IO>(z));
         push<W, V>(win, x);
         if (on) stc<IO, V>(a.y, at, z);
         at += a.C;
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm<V>) conv_bwd_kernel(ConvAr
         const Vec<V> x = ldc<IO, V>(xs, i * kCh<V>);
         Vec<V> dz = ldc<IO, V>(ds, i * kCh<V>);
         if (a.silu) {
-          const Vec<V> z = taps.z(win, x), g = sigmoids(z);
+          const Vec<V> z = taps.z(win, x), g = sigmoids<IO>(z);
 #pragma unroll
           for (int h = 0; h < V; ++h)  // g (1 + z (1 - g))
             dz.p[h] = mul2(dz.p[h], mul2(g.p[h], fma2(z.p[h], fma2(both(-1.f), g.p[h], both(1.f)),
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a) {
   for (int j = 0; j < W - 1; ++j) win[j] = ldc<IO, V>(a.state_T, st + (int64_t)j * a.C);
   const Taps<IO, W, V> taps(a, c);
   Vec<V> z = taps.z(win, x);
-  if (a.silu) z = mulc(z, sigmoids(z));
+  if (a.silu) z = mulc(z, sigmoids<IO>(z));
   push<W, V>(win, x);
   stc<IO, V>(a.y, i, z);
 #pragma unroll

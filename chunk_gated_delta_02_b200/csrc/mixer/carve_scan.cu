@@ -76,7 +76,7 @@ struct ScanArgs {
 // tokens.  Close to zero both therefore come from the series of exp(u) - 1:
 // four terms within 1/16 (the first one left out is below 2^-27), six within
 // 1/4 where 1 - exp(u) needs its own relative accuracy (below 2^-24 of it).
-template <bool REST>
+template <typename IO, bool REST>
 __device__ __forceinline__ void decays(float2 u, float2& a, float2& rest) {
   constexpr float kNear = REST ? 0.25f : 0.0625f;
   float2 p = both(1.f / 24);
@@ -84,28 +84,27 @@ __device__ __forceinline__ void decays(float2 u, float2& a, float2& rest) {
   p = fma2(u, p, both(1.f / 6));
   p = fma2(u, p, both(0.5f));
   p = fma2(u, p, both(1.f));
-  const float2 l = mul2(u, both(kLog2e));
-  const float ex = ex2(l.x), ey = ex2(l.y);
+  const float2 e = exp_of<IO>(u);
   const bool nx = fabsf(u.x) < kNear, ny = fabsf(u.y) < kNear;
   if (REST) {
     const float2 m = mul2(u, p);  // exp(u) - 1
-    rest.x = nx ? -m.x : 1.f - ex;
-    rest.y = ny ? -m.y : 1.f - ey;
+    rest.x = nx ? -m.x : 1.f - e.x;
+    rest.y = ny ? -m.y : 1.f - e.y;
     p = add2(m, both(1.f));
   } else {
     p = fma2(u, p, both(1.f));
   }
-  a.x = nx ? p.x : ex;
-  a.y = ny ? p.y : ey;
+  a.x = nx ? p.x : e.x;
+  a.y = ny ? p.y : e.y;
 }
 
 // The fused activation u = -s softplus(g) of a pair, and with SLOPE its
 // derivative -s sigmoid(g).  softplus(g) = max(g, 0) + log(1 + e) with e =
 // exp(-|g|) <= 1; log(1 + e) / e on [0, 1] is a polynomial of degree 8 fitted
 // for the least largest relative error (3e-8; below 1.5e-7 in fp32).
-template <bool SLOPE>
+template <typename IO, bool SLOPE>
 __device__ __forceinline__ float2 activated(float2 g, float s, float2& slope) {
-  const float2 e = make_float2(ex2(-kLog2e * fabsf(g.x)), ex2(-kLog2e * fabsf(g.y)));
+  const float2 e = exp_of<IO>(make_float2(-fabsf(g.x), -fabsf(g.y)));
   float2 p = fma2(e, both(0.005232689436525106f), both(-0.02950522117316723f));
   p = fma2(e, p, both(0.07822592556476593f));
   p = fma2(e, p, both(-0.13663244247436523f));
@@ -123,10 +122,10 @@ __device__ __forceinline__ float2 activated(float2 g, float s, float2& slope) {
 }
 
 // The decay of a gate pair, 1 minus it, and the slope of the activation.
-template <bool ACT, bool REST, bool SLOPE>
+template <typename IO, bool ACT, bool REST, bool SLOPE>
 __device__ __forceinline__ void gate(float2 g, float s, float2& a, float2& rest,
                                      float2& slope) {
-  decays<REST>(ACT ? activated<SLOPE>(g, s, slope) : g, a, rest);
+  decays<IO, REST>(ACT ? activated<IO, SLOPE>(g, s, slope) : g, a, rest);
 }
 
 // The state after a segment from the one before it.  A segment that starts a
@@ -341,7 +340,7 @@ template <bool ACT, bool COMP, typename IO>
 __device__ __forceinline__ void token(const IO* x, const IO* g, int at, float s,
                                       float2& d, float2& v) {
   float2 rest, slope;
-  gate<ACT, COMP, false>(ld2(g + at), s, d, rest, slope);
+  gate<IO, ACT, COMP, false>(ld2(g + at), s, d, rest, slope);
   v = ld2(x + at);
   if (COMP) v = mul2(v, rest);
 }
@@ -823,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a) {
       if (M && end) r_in = ld_state(a.dh_T, p.seq0 + e->last, a.C, c);
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        gate<ACT, COMP, ACT>(ld2(st.g + at0 + i * kCh), a.dscale, da[i], rest[i], slope[i]);
+        gate<IO, ACT, COMP, ACT>(ld2(st.g + at0 + i * kCh), a.dscale, da[i], rest[i], slope[i]);
         float2 u = ld2(st.x + at0 + i * kCh);
         if (COMP) u = mul2(u, rest[i]);
         if (M && (start >> i & 1)) A = both(1.f), H = both(0.f);
@@ -956,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a) {
         if (SEG && (end >> i & 1))
           r = ld_state(a.dh_T, p.seq0 + seq_of(p.b, t), a.C, c);
         float2 f, k, sl;
-        gate<ACT, COMP, ACT>(ld2(st.g + at), a.dscale, f, k, sl);
+        gate<IO, ACT, COMP, ACT>(ld2(st.g + at), a.dscale, f, k, sl);
         float2 ox = add2(ld2(st.d + at), r);
         r = mul2(f, ox);
         float2 og = mul2(r, COMP ? fma2(ld2(st.x + at), both(-1.f), hp[i]) : hp[i]);
@@ -997,7 +996,7 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs a) {
   const float2 gv = ld2(static_cast<const IO*>(a.g) + b * a.gp + c);
   float2 u = ld2(static_cast<const IO*>(a.x) + b * a.xp + c);
   float2 h = ld2(a.h_T + i), e, rest, slope;
-  gate<ACT, true, false>(gv, a.dscale, e, rest, slope);
+  gate<IO, ACT, true, false>(gv, a.dscale, e, rest, slope);
   if (a.comp) u = mul2(u, rest);
   h = fma2(e, h, u);
   st2(a.h_T + i, h);
