@@ -344,7 +344,9 @@ carve_status carve_decode_step(const carve_shape* shape,
  * C channels (a multiple of 8); heads are contiguous channels.  g is the
  * log-decay (g <= 0), or with decay_scale s > 0 raw decay logits a with
  * g = -s softplus(a) (as in carve_shape).  dtype is that of x, g, h, d_h,
- * dx and dg; states are fp32.
+ * dx and dg; states are fp32.  A log-decay of -infinity forgets a finite
+ * state; an infinite or NaN one makes its sequence NaN from there on, and no
+ * other.
  */
 typedef struct {
   int32_t B, T, C;
