@@ -160,7 +160,7 @@ def fwd_path(shape):
     return None if r is None else r.decode()
 
 
-def _check(t, name, dtype, shape, device, contiguous=True):
+def _check(t, name, dtype, shape, device):
     if t is None:
         raise ValueError("%s is required" % name)
     if not t.is_cuda:
@@ -172,7 +172,7 @@ def _check(t, name, dtype, shape, device, contiguous=True):
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, expected %s"
                          % (name, tuple(t.shape), tuple(shape)))
-    if contiguous and not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
 
 
