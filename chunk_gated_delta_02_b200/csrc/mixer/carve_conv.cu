@@ -17,6 +17,9 @@
 // backward (5.1 TB/s of x, dy and dx: two streams in and one out, at 54 % of the
 // issue slots; twice the warps with half the registers were no faster).
 // Without the rings (loads into registers a row ahead) they took 177 and 332.
+// Packed sequences are walked one after another by a warp, each with its search
+// and its ring's start: 32768 x 6144 in 500 sequences takes 167 and 330 us, in
+// 4000 of them 317 and 709, where the bytes take 125 and 187.
 #include "mixer_common.cuh"
 
 namespace carve {

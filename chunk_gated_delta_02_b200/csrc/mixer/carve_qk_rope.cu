@@ -16,7 +16,11 @@
 // forward (6.5 TB/s of the rows in and out, what a plain copy reaches) and 270
 // us backward with the weights' gradients (6.0 TB/s of 6 tensors); issue is at
 // 74 and 69 %, so both are near its limit too.  With loads into registers in
-// place of the rings they took 191 and 332.
+// place of the rings they took 191 and 332.  Widths that are not 8 times a
+// power of two leave lanes of a group without elements, which load and sum all
+// the same, and issue is then the bound: 16384 x (12 + 12) x 80 takes 43 and 79
+// us where its bytes take 19.5 and 29, x 96 37 and 67 (23 and 35), and (8 + 8)
+// x 192 54 and 93 (31 and 47).
 #include "mixer_common.cuh"
 
 namespace carve {
@@ -72,7 +76,8 @@ struct Lane {
 };
 
 // cos and sin of the lane's 4 angles: the angle in turns, reduced in fp64
-// (positions of a million still leave 2^-29 of a turn), then fp32.
+// (off by 2^-52 of the turns: 2^-34 of one at a million positions, 2^-23 at
+// 2^31), then fp32.
 __device__ __forceinline__ void angles(const RopeArgs& a, int l, int64_t token,
                                        Q& c, Q& s) {
   const double p = (double)a.pos[token] * 0.15915494309189533577;  // 1 / (2 pi)

@@ -27,12 +27,17 @@
 // What bounds it (bf16, 6.47 TB/s of measured copy bandwidth): 8 x 4096 x 2048
 // forward 70 us, 5.7 TB/s of x, g and h, at 19.5 instructions an element and
 // 58 % of the issue slots: memory and issue together.  With activation and
-// complement 112 us: the polynomials, 33 instructions an element.  Backward
-// 117 us, 5.7 TB/s of its 5 tensors; with activation and complement 197 us,
-// 60 instructions an element, issue.  Packed rows add the borders, whose
-// segments a cluster waits for: 57 us forward, 104 backward, where one
-// sequence of as many tokens takes 47 and 74, and the bytes 31 and 52 (16384
-// tokens x 2048 in 33 sequences with states).
+// complement 109 us: the polynomials, 33 instructions an element; no unit is
+// full (issue 60 %, the heavy half of the FMA pipe 61 %, DRAM 39 %), and the
+// warps' first stall is the math pipes.  Backward 117 us, 5.7 TB/s of its 5
+// tensors; with activation and complement 195 us, 60 instructions an
+// element (62 %, 56 % and 39 %).  Packed rows add the borders, whose
+// segments a cluster waits for: 57 us forward, 94 to 104 backward, where one
+// sequence of as many tokens takes 47 and 75, and the bytes 31 and 52 (16384
+// tokens x 2048 in 33 sequences with states).  With a border every 65 tokens
+// nearly every step waits: 239 and 320 us for 500 sequences in 32768 x 2048,
+// whose bytes take 62 and 104.  Few channels leave SMs without a block: 110 and
+// 199 us for 1 x 65536 x 512, bytes 31 and 52.
 #include "mixer_common.cuh"
 
 #include <cooperative_groups.h>

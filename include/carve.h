@@ -414,7 +414,8 @@ carve_status carve_scan_step(const carve_scan_shape* shape, const void* x,
  *
  * for the RD / 2 pairs (i, j = i + RD / 2), or (2 i, 2 i + 1) with
  * interleaved != 0, of the first RD elements; the others keep n.  The angle
- * is formed and reduced in fp64, so far positions keep full accuracy.  A
+ * is formed and reduced in fp64: it is off by about 2^-52 of itself, which
+ * fp32 does not see below 2^27 or so and which is 7e-7 radians at 2^31.  A
  * row whose norm is 0 with eps = 0 gives zeros (and a zero gradient).  A NaN
  * makes its whole row NaN.  The sum of squares is formed in fp32: it has to be
  * finite (elements below 1e18).  With eps = 0 the squares of elements below
