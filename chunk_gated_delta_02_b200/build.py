@@ -125,7 +125,8 @@ def build(force=False, verbose=False):
     if force or _binding_stale():
         lacks = _binding_lacks()
         if lacks:
-            print("note: %s is not here, so %s is not built; %s is complete"
+            print("note: %s is not here, so %s is not built (one that is there "
+                  "stays as it was); %s is complete"
                   % (lacks, os.path.basename(BINDING), LIB), file=sys.stderr)
             return LIB
         tmp = BINDING + ".tmp.%d" % os.getpid()
